@@ -12,8 +12,9 @@
 // too: a power of two brings the row's largest to [128, 256), and the 8 significant bits of a
 // bf16 value fit down to 2^-31 of that.
 //   Output.  mma m16n8k16 on the values widened to fp16 (exact); p * vs is rounded to fp16
-// (2^-11) after a power of two, per row and 32 tokens, that brings the largest to
-// [2^14, 2^15), so no size of the values can leave fp16's range.
+// (2^-11) after a power of two that keeps the largest that the row has had from this warp, as
+// weighted against the present maximum, in [2^14, 2^15): what is lost lies below 2^-39 of it,
+// whatever the size of the values.
 // The tokens of all sequences form one list of tiles, cut into equal runs, one to a block, so
 // that ragged batches and one long sequence fill the GPU alike; a sequence that a cut divides
 // leaves partial results (maximum, sum, output) that a second kernel joins in order.
@@ -445,11 +446,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             }
           }
         }
-        // ---- softmax.  The reference maximum moves only when a score passes it by 2^8, and
-        // the power of two that brings p * vs into fp16 only when one would pass 2^15, so the
-        // output is rescaled rarely and the MMAs add straight into it.
+        // ---- softmax.  The reference maximum moves only when a score passes it by 8 (in base
+        // 2), and the power of two that brings p * vs into fp16 only when one would pass 2^15 or
+        // when the reference moves, so the output is rescaled rarely and the MMAs add straight
+        // into it.  References are whole numbers: what came before falls by 2^-drop exactly, and
+        // the range that it needed falls as much.  A range that only ever rose would go on
+        // holding a large value that has lost its weight, and drop what has taken it.
         uint32_t pf[ROWS / 8][4];
-        float factor[ROWS / 8];
+        float factor[ROWS / 8];  // of the outputs
         bool moved = false;
 #pragma unroll
         for (int half = 0; half < ROWS / 8; ++half) {
@@ -459,8 +463,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const bool up_m = mx > m_ref[half] + 8.0f;
-          const float mn = up_m ? mx : m_ref[half];
-          factor[half] = up_m ? exp2_approx(m_ref[half] - mn) : 1.0f;
+          const float mn = up_m ? ceilf(mx) : m_ref[half];
+          const int drop = up_m ? static_cast<int>(fminf(mn - m_ref[half], 1024.0f)) : 0;
+          l_run[half] *= up_m ? exp2_approx(m_ref[half] - mn) : 1.0f;
           m_ref[half] = mn;
           float sum = 0.0f, top = 0.0f;
           float pv[4][2];
@@ -476,16 +481,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
               top = fmaxf(top, fabsf(pv[j][i]));
             }
           }
-          l_run[half] = fmaf(l_run[half], factor[half], sum);
+          l_run[half] += sum;
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
           const int e = static_cast<int>(__float_as_uint(top) >> 23) - 14;
-          if (e > scale_exp[half]) {  // down by 2^(e - scale_exp)
-            factor[half] *= __uint_as_float(
-                static_cast<uint32_t>(max(0, 127 + scale_exp[half] - e)) << 23);
-            scale_exp[half] = e;
-          }
-          moved |= factor[half] != 1.0f;
+          const int range = max(max(1, scale_exp[half] - drop), e);
+          const int shift = drop + range - scale_exp[half];  // down by 2^shift; none below 0
+          factor[half] = __uint_as_float(static_cast<uint32_t>(max(0, 127 - shift)) << 23);
+          scale_exp[half] = range;
+          moved |= shift != 0;
           const float up = __uint_as_float(static_cast<uint32_t>(254 - scale_exp[half]) << 23);
 #pragma unroll
           for (int j = 0; j < 4; ++j) pf[half][j] = pack_f16x2(pv[j][0] * up, pv[j][1] * up);

@@ -1,0 +1,95 @@
+"""Single-token attention over the whole range of scores and values: scores that rise and fall
+along a sequence, value scales far apart.  Float32 outputs against the 64-bit form, within the
+bounds counted in attention_bounds."""
+
+import math
+
+import pytest
+import torch
+
+import attention_bounds as tight
+import decode_ref as ref
+from test_gpu_attention_decode import _gen, _run, _setup
+from util import DEV
+
+pytestmark = pytest.mark.gpu
+
+LAYOUTS = [(16, 4), (32, 2)]            # groups of 4 and of 16 query rows
+# (lengths, prefix): undivided sequences, divided ones, a prefix of under 64 query rows a head;
+# long enough for several tiles to a block
+PLACES = {"undivided": ([1000, 129, 37, 640], None), "divided": ([40000, 700, 1, 3000], None),
+          "prefix": ([100, 1, 0], 20000)}
+
+
+def _check(fge, s, prefix, scale=None, unit=tight.OWN, **more):
+    q, cache, table, lens, pp = s
+    out, lse, status = _run(fge, q, cache, table, lens, pp, prefix, torch.float32, scale)
+    assert status == 0
+    r = tight.attention(q, cache, table, lens, q.shape[2] ** -0.5 if scale is None else scale, pp,
+                        prefix or 0, unit, **more)
+    ref.check_attention(out, lse, r, torch.float32)
+
+
+def _no_zero_rows(cache):
+    """A value in every row: a cache's zero rows have a scale of their own."""
+    cache[2][(cache[2] & 0x7F).amax(-1) == 0] = 0x38
+
+
+def _along(s, prefix):
+    """Place of every cached token in its sequence, 0 to 1, as [pages, page]."""
+    q, cache, table, lens, pp = s
+    page = cache[1].shape[2]
+    at = torch.zeros((cache[1].shape[0], page), device=DEV)
+    rows = [(table[i], int(lens[i])) for i in range(len(lens))]
+    if pp is not None:
+        rows.append((pp, prefix))
+    for pages, n in rows:
+        for j in range((n + page - 1) // page):
+            at[int(pages[j])] = (j * page + torch.arange(page, device=DEV)) / n
+    return at
+
+
+@pytest.mark.parametrize("heads,n_kv", LAYOUTS)
+@pytest.mark.parametrize("place", PLACES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rise,spread", [(64.0, 0.0), (1.0 / 64.0, 0.0), (1.0, 20.0), (8.0, 40.0),
+                                         (64.0, -40.0)])
+def test_scores_and_values_that_change_along_it(fge, heads, n_kv, place, d, rise, spread):
+    # spread < 0: values that fall by 2^(2 spread) along the sequence
+    lengths, prefix = PLACES[place]
+    s = _setup(fge, lengths, heads, n_kv, d, 64, int(d + spread), prefix, spoil=False)
+    cache = s[1]
+    _no_zero_rows(cache)
+    at = _along(s, prefix)[:, None]
+    cache[1].mul_(torch.exp(math.log(rise) * at))
+    if spread < 0:
+        cache[3].mul_(torch.exp2(-spread * (1 - 2 * at)))
+    else:
+        cache[3].mul_(torch.exp2(spread * (2 * torch.rand(cache[3].shape, generator=_gen(5),
+                                                          device=DEV) - 1)))
+    _check(fge, s, prefix)
+
+
+@pytest.mark.parametrize("place", PLACES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("up,down", [(20, 20), (40, 28), (60, 40), (120, 90), (300, 100)])
+def test_a_large_value_that_loses_its_weight(fge, place, d, up, down):
+    # The first token has the largest value; another one, whose score is `up` higher in base 2
+    # and whose value is 2^down smaller, takes its weight.  Both lie in the part of the tiles
+    # that one warp takes.
+    _, prefix = PLACES[place]
+    n = {"undivided": 200, "divided": 60000, "prefix": 16384}[place]
+    lengths, shared = ([n, 130], None) if prefix is None else ([1, 1], n)
+    s = _setup(fge, lengths, 4, 2, d, 64, 17, shared, spoil=False)
+    q, cache, table, lens, pp = s
+    q.fill_(1.0)
+    _no_zero_rows(cache)
+    cache[0].zero_()                    # score 0 but for the one token
+    cache[1].fill_(1.0)
+    cache[3].fill_(2.0 ** -down)
+    pages = table[0] if shared is None else pp
+    cache[3][int(pages[0]), :, 0] = 1.0
+    late = (int(pages[128 // 64]), slice(None), 128 % 64)
+    cache[0][late] = 0x38               # 1.0
+    cache[1][late] = up * math.log(2.0) / d
+    _check(fge, s, shared, scale=1.0)
