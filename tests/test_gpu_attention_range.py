@@ -1,6 +1,6 @@
 """Single-token attention over the whole range of scores and values: scores that rise and fall
-along a sequence, value scales far apart.  Float32 outputs against the 64-bit form, within the
-bounds counted in attention_bounds."""
+along a sequence, value scales far apart, rows of value zero.  Float32 outputs against the
+64-bit form, within the bounds counted in attention_bounds."""
 
 import math
 
@@ -93,3 +93,26 @@ def test_a_large_value_that_loses_its_weight(fge, place, d, up, down):
     cache[0][late] = 0x38               # 1.0
     cache[1][late] = up * math.log(2.0) / d
     _check(fge, s, shared, scale=1.0)
+
+
+@pytest.mark.parametrize("heads,n_kv", LAYOUTS)
+@pytest.mark.parametrize("place", PLACES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("small", [1.0, 2.0 ** -20, 2.0 ** -31, 2.0 ** -60])
+def test_rows_of_value_zero_beside_small_values(fge, heads, n_kv, place, d, small):
+    # every 13th row is zero and has scale 1 by the cache's rule
+    lengths, prefix = PLACES[place]
+    s = _setup(fge, lengths, heads, n_kv, d, 64, d, prefix, spoil=False)
+    cache = s[1]
+    zero = (cache[2] & 0x7F).amax(-1) == 0
+    assert zero.any() and (cache[3][zero] == 1.0).all()
+    cache[3][~zero] *= small
+    _check(fge, s, prefix)
+
+
+def test_only_rows_of_value_zero(fge):
+    s = _setup(fge, [300, 40, 1], 16, 4, 128, 64, 3, spoil=False)
+    s[1][2].zero_()
+    s[1][3].fill_(1e30)
+    out, lse, status = _run(fge, *s[:4], dtype=torch.float32)
+    assert status == 0 and not out.any() and torch.isfinite(lse).all()
