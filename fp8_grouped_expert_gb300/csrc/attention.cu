@@ -410,8 +410,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       for (int i = 0; i < D / 8; ++i) m = max(m, max((x[i] >> 16) & 0x7FFFu, x[i] & 0x7FFFu));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      // 2^k brings the largest value to [128, 256); biased exponents, kept normal
-      const int up = min(254, max(1, 134 + 127 - static_cast<int>(m >> 7)));
+      // 2^k brings the largest value to [128, 256); biased exponents, both factors kept normal
+      const int up = min(253, max(1, 134 + 127 - static_cast<int>(m >> 7)));
       const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
       row_scale[half] = __uint_as_float(static_cast<uint32_t>(254 - up) << 23) * a.scale *
                         1.4426950408889634f;

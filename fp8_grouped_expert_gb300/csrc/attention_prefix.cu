@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 4; ++j) m = max(m, max((w4[j] >> 16) & 0x7FFFu, w4[j] & 0x7FFFu));
 #pragma unroll
         for (int d = 1; d < kLanes; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const int up = min(254, max(1, 134 + 127 - static_cast<int>(m >> 7)));
+        const int up = min(253, max(1, 134 + 127 - static_cast<int>(m >> 7)));
         const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
         if (lane % kLanes == 0)
           tops[r0 + i * kRowsLoad] = __uint_as_float(static_cast<uint32_t>(254 - up) << 23) *
@@ -514,8 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 16; j += 4) {
               const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(sc + 16 * c + j);
               const ulonglong2 lv = *reinterpret_cast<const ulonglong2*>(sc + kTile + 16 * c + j);
-              const float2 u = unpair(fma2(mul2(pair_bits(r[j], r[j + 1]), ks.x), rs2, lv.x));
-              const float2 v = unpair(fma2(mul2(pair_bits(r[j + 2], r[j + 3]), ks.y), rs2, lv.y));
+              // the row's factor times the key's first: a score times a large key's scale alone
+              // can pass float's range
+              const float2 u = unpair(fma2(mul2(ks.x, rs2), pair_bits(r[j], r[j + 1]), lv.x));
+              const float2 v = unpair(fma2(mul2(ks.y, rs2), pair_bits(r[j + 2], r[j + 3]), lv.y));
               top = fmaxf(fmaxf(top, fmaxf(u.x, u.y)), fmaxf(v.x, v.y));
             }
           }
@@ -555,9 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const ulonglong2 vs = *reinterpret_cast<const ulonglong2*>(sc + 2 * kTile + 16 * c + j);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              float2 e = unpair(fma2(mul2(pair_bits(r[j + 2 * h], r[j + 2 * h + 1]),
-                                          h ? ks.y : ks.x),
-                                     rs2, minus2));
+              float2 e = unpair(fma2(mul2(h ? ks.y : ks.x, rs2),
+                                     pair_bits(r[j + 2 * h], r[j + 2 * h + 1]), minus2));
               e.x = exp2_approx(e.x);
               e.y = exp2_approx(e.y);
               if (!full) {

@@ -1,6 +1,6 @@
 """Single-token attention over the whole range of scores and values: scores that rise and fall
-along a sequence, value scales far apart, rows of value zero.  Float32 outputs against the
-64-bit form, within the bounds counted in attention_bounds."""
+along a sequence, value scales far apart, rows of value zero, tiny queries.  Float32 outputs
+against the 64-bit form, within the bounds counted in attention_bounds."""
 
 import math
 
@@ -116,3 +116,16 @@ def test_only_rows_of_value_zero(fge):
     s[1][3].fill_(1e30)
     out, lse, status = _run(fge, *s[:4], dtype=torch.float32)
     assert status == 0 and not out.any() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("prefix,b", [(None, 3), (700, 3), (700, 40)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power", [-110, -121, -126])
+def test_tiny_queries_and_large_keys(fge, prefix, b, d, power):
+    s = _setup(fge, [(97 * i) % 300 for i in range(b)], 16, 4, d, 64, 23, prefix, spoil=False)
+    q, cache, table, lens, pp = s
+    q.copy_((q.float() * 2.0 ** power).to(torch.bfloat16))
+    cache[1].mul_(2.0 ** 118)           # values up to 2^121
+    # the row's factor may be subnormal: 2^-129 keeps 20 bits
+    _check(fge, s, prefix, scale=0.25 * 2.0 ** (-118 - power),
+           unit=tight.TCGEN05 if b * 4 >= 64 else tight.OWN, score_error=2.0 ** -19)
