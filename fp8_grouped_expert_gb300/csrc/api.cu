@@ -204,6 +204,7 @@ size_t fge_workspace_bytes(fge_op op, int64_t a, int64_t b, int64_t c, int E, in
     }
     case FGE_OP_ATTENTION_DECODE:
     case FGE_OP_ATTENTION_DECODE_SHARED:
+      if (b < 0 || b > INT32_MAX || c < 0 || c > INT32_MAX) return kWsHeaderBytes;
       return kWsHeaderBytes + attention_scratch_bytes(a, static_cast<int>(b), static_cast<int>(c),
                                                       E, op == FGE_OP_ATTENTION_DECODE_SHARED);
     case FGE_OP_MOE_DECODE: return kWsHeaderBytes + moe_decode_scratch_bytes(a, b, c, E, k);
