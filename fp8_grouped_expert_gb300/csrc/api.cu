@@ -701,8 +701,8 @@ fge_status fge_moe_layer_decode(const float* logits, const void* x, int64_t T, i
   FGE_CHECK(cur_device_ok());
   FGE_REQUIRE(format == FGE_W4_LUT || format == FGE_W4_SUBNORMAL, FGE_ERR_INVALID_ARG);
   FGE_REQUIRE(out_dtype == FGE_DTYPE_BF16 || out_dtype == FGE_DTYPE_F32, FGE_ERR_INVALID_ARG);
-  FGE_REQUIRE(T >= 0 && T <= kMoeDecodeTokens && H > 0 && H % 128 == 0 && H <= 8192 && I > 0 &&
-                  I % 128 == 0 && I <= 8192,
+  FGE_REQUIRE(T >= 0 && T <= kMoeDecodeTokens && H > 0 && H % 128 == 0 && H <= kMoeDecodeWidth &&
+                  I > 0 && I % 128 == 0 && I <= kMoeDecodeWidth,
               FGE_ERR_BAD_SHAPE);
   FGE_REQUIRE(E >= 1 && E <= kMaxExperts && k >= 1 && k <= E && k <= 32, FGE_ERR_BAD_SHAPE);
   if (T == 0) return FGE_OK;
@@ -790,7 +790,7 @@ static fge_status attention_common(const void* q, int64_t q_stride, int64_t B, i
   FGE_CHECK(cache_args(cache, &c));
   FGE_REQUIRE(out_dtype == FGE_DTYPE_BF16 || out_dtype == FGE_DTYPE_F32, FGE_ERR_INVALID_ARG);
   FGE_REQUIRE(n_heads >= 1 && n_heads <= 65536 && n_heads % c.n_kv == 0, FGE_ERR_BAD_SHAPE);
-  FGE_REQUIRE(B >= 0 && B <= 65536 && B * n_heads < (1LL << 24), FGE_ERR_BAD_SHAPE);
+  FGE_REQUIRE(B >= 0 && B <= kAttentionBatch && B * n_heads < kAttentionRows, FGE_ERR_BAD_SHAPE);
   FGE_REQUIRE(table_width >= 0 && table_width < (1LL << 31) / c.page_size && prefix_width >= 0 &&
                   prefix_width < (1LL << 31) / c.page_size,
               FGE_ERR_BAD_SHAPE);

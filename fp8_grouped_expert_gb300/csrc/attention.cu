@@ -985,7 +985,10 @@ cudaError_t run_attention(const AttentionArgs& a, void* scratch, cudaStream_t s)
 }  // namespace
 
 size_t attention_scratch_bytes(int64_t B, int n_heads, int head_dim, int n_kv, bool shared) {
-  if (B <= 0 || n_heads <= 0 || head_dim <= 0 || n_kv <= 0 || n_heads % n_kv != 0) return 0;
+  // what the call refuses needs nothing
+  if (B <= 0 || B > kAttentionBatch || n_heads <= 0 || B * n_heads >= kAttentionRows ||
+      head_dim <= 0 || n_kv <= 0 || n_heads % n_kv != 0)
+    return 0;
   const int64_t group = n_heads / n_kv, rows = group <= 8 ? 8 : 16;
   size_t n = 2 * static_cast<size_t>(blocks_of_list()) * rows;
   if (shared) {

@@ -155,6 +155,7 @@ cudaError_t launch_kv_write(const uint16_t* k, int64_t k_stride, const uint16_t*
 cudaError_t launch_kv_read(const int64_t* slots, int64_t T, const KvCacheArgs& c, int out_f32,
                            void* k_out, void* v_out, int32_t* status, cudaStream_t s);
 
+constexpr int64_t kAttentionBatch = 65536, kAttentionRows = 1 << 24;  // B, and below: B n_heads
 // Attention of B single tokens over the cache; prefix_pages null: no shared prefix.
 struct AttentionArgs {
   const uint16_t* q;         // [B, n_heads * head_dim], rows q_stride apart
@@ -177,7 +178,8 @@ struct AttentionArgs {
 size_t attention_scratch_bytes(int64_t B, int n_heads, int head_dim, int n_kv, bool shared);
 cudaError_t launch_attention_decode(const AttentionArgs& a, void* scratch, cudaStream_t s);
 
-constexpr int kMoeDecodeTokens = 64;  // the few-token layer's limit
+constexpr int kMoeDecodeTokens = 64;  // the few-token layer's limits
+constexpr int kMoeDecodeWidth = 8192;
 struct MoeDecodeArgs {
   const float* logits;
   const uint16_t* x;

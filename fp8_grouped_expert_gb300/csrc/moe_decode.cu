@@ -1231,7 +1231,10 @@ cudaError_t run_tokens(const MoeDecodeArgs& a, const Ws& w, cudaStream_t s) {
 }  // namespace
 
 size_t moe_decode_scratch_bytes(int64_t T, int64_t H, int64_t I, int E, int k) {
-  if (T < 0 || H < 0 || I < 0 || E < 0 || k < 0) return 0;
+  // what the call refuses needs nothing
+  if (T < 0 || T > kMoeDecodeTokens || H < 0 || H > kMoeDecodeWidth || I < 0 ||
+      I > kMoeDecodeWidth || E < 0 || E > kMaxExperts || k < 0 || k > E || k > 32)
+    return 0;
   return carve(nullptr, T, H, I, E, k).bytes;
 }
 

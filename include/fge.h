@@ -102,8 +102,8 @@ fge_status fge_init(int device);
 /* Human-readable name of a status code (static string). */
 const char* fge_status_string(fge_status status);
 
-/* Workspace bytes an operation needs for the given sizes (0 for a bad op; heads that are no
- * multiple of the key/value heads, which the call refuses: the status header alone). */
+/* Workspace bytes an operation needs for the given sizes (0 for a bad op; shapes that a
+ * decode-step call refuses: the status header alone). */
 size_t fge_workspace_bytes(fge_op op, int64_t a, int64_t b, int64_t c, int E, int k);
 
 /* Host-side ledger of this process's calls into the library (counted from library load

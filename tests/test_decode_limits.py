@@ -34,3 +34,19 @@ def _bytes(op, *args):
 def test_heads_that_are_no_groups_need_no_scratch(heads, n_kv):
     for op in (fge.OP_ATTENTION_DECODE, fge.OP_ATTENTION_DECODE_SHARED):
         assert _bytes(op, 2, heads, 128, n_kv) == HEADER
+
+
+@pytest.mark.parametrize("t,h,inter,e,k", [(65, 256, 128, 8, 2), (1 << 20, 4096, 1536, 128, 8),
+                                           (4, 256, 128, 8, 1 << 30), (4, 256, 128, 8, 9),
+                                           (4, 1 << 40, 128, 8, 2), (4, 256, 8320, 8, 2),
+                                           (4, 256, 128, 513, 2)])
+def test_layers_that_are_refused_need_no_scratch(t, h, inter, e, k):
+    # the binding allocates a workspace before the call looks at the shape
+    assert fge.workspace_bytes(fge.OP_MOE_DECODE, t, h, inter, e, k) == HEADER
+
+
+def test_batches_that_are_refused_need_no_scratch():
+    for op in (fge.OP_ATTENTION_DECODE, fge.OP_ATTENTION_DECODE_SHARED):
+        assert fge.workspace_bytes(op, 65537, 16, 128, 4) == HEADER
+        assert fge.workspace_bytes(op, 65536, 256, 128, 4) == HEADER
+        assert fge.workspace_bytes(op, 65535, 256, 128, 4) > HEADER
