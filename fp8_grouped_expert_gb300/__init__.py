@@ -551,7 +551,8 @@ def _load_decode():
 
 
 def _late(name):
-    """Stands in for a call where the package was imported before it was built."""
+    """Stands in for a call until the first use of the library: what is loaded at import would stay
+    when build() replaces it."""
     def call(*args, **kwargs):
         lib()
         return globals()[name](*args, **kwargs)
@@ -561,10 +562,6 @@ def _late(name):
 
 _DECODE_CALLS = ("kv_cache_write", "kv_cache_read", "attention_decode", "moe_layer_decode")
 kv_cache_write, kv_cache_read, attention_decode, moe_layer_decode = map(_late, _DECODE_CALLS)
-try:
-    _load_decode()
-except ImportError:
-    pass  # not built yet, or for another torch: lib() says so
 
 
 # ------------------------------------------------------- single-token attention and its cache
