@@ -108,12 +108,11 @@ def lib():
             fn = getattr(handle, name)
             fn.argtypes = args
             fn.restype = _RESTYPES.get(name, ctypes.c_int)
+        _lib = handle
         try:
             _load_decode()
-        except ImportError as e:
-            raise FgeError("_decode.so is not built (run fp8_grouped_expert_gb300.build.build()): "
-                           "%s" % e)
-        _lib = handle
+        except ImportError:
+            pass  # the calls through ctypes do without it; those that need it say so
     return _lib
 
 
@@ -555,6 +554,13 @@ def _late(name):
     when build() replaces it."""
     def call(*args, **kwargs):
         lib()
+        if globals()[name] is call:
+            try:
+                _load_decode()
+            except ImportError as e:
+                raise FgeError("%s needs _decode.so, which does not load (not built, or built for "
+                               "another torch than %s: run fp8_grouped_expert_gb300.build.build()): "
+                               "%s" % (name, torch.__version__, e))
         return globals()[name](*args, **kwargs)
     call.__name__ = call.__qualname__ = name
     return call

@@ -40,3 +40,22 @@ def test_a_decode_call_loads_what_it_needs():
             "    except f.FgeError as e:\n"
             "        assert 'cache' in str(e), e\n"
             "assert inspect.isbuiltin(f.kv_cache_read) and inspect.isbuiltin(f.moe_layer_decode)\n")
+
+
+def test_calls_through_ctypes_do_without_the_binding():
+    # as where it was built for another torch
+    out = _python(
+        "import sys, torch\n"
+        "sys.modules['fp8_grouped_expert_gb300._decode'] = None     # importing it fails\n"
+        "import fp8_grouped_expert_gb300 as f\n"
+        "assert f.lib().fge_version() > 0 and f.workspace_bytes(f.OP_MOE_LAYER, 1, 128, 128, 1, 1)\n"
+        "x = torch.zeros((1, 128), dtype=torch.bfloat16)\n"
+        "for call in (lambda: f.fp8_quant_act(x), lambda: f.moe_layer_decode(1, x),\n"
+        "             lambda: f.kv_cache_read(x, None), lambda: f.attention_decode(q=x)):\n"
+        "    try:\n"
+        "        call()\n"
+        "        raise SystemExit('not refused')\n"
+        "    except f.FgeError as e:\n"
+        "        print(e)\n").splitlines()
+    assert "CUDA" in out[0] and len(out) == 4
+    assert all("_decode" in line and "torch" in line for line in out[1:])
