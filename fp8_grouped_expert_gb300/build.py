@@ -66,14 +66,24 @@ def compile_binding():
 
 
 def link_binding(obj):
+    """Links the binding from that object if it changed or another torch's is linked."""
     import torch
-    if _stale([obj, LIB], BINDING):
+    record = os.path.join(BUILD, "binding-linked.txt")  # the object that BINDING is from
+    linked = None
+    if os.path.exists(record):
+        with open(record) as f:
+            linked = f.read()
+    if linked != obj or _stale([obj, LIB], BINDING):
         tmp = BINDING + ".tmp"
         _run(["g++", "-shared", "-o", tmp, obj,
               "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python",
               "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libfge.so",
               "-Wl,-rpath,$ORIGIN"])
+        if linked is not None:
+            os.remove(record)  # whatever happens between here and its rewriting, link again
         os.replace(tmp, BINDING)
+        with open(record, "w") as f:
+            f.write(obj)
 
 
 def build(verbose=False, ptxas_info=False):
