@@ -64,7 +64,7 @@ struct Segment {
 };
 
 // Tiles of a sequence: at least one, so that every row is written.
-__device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kTile - 1) / kTile); }
+__device__ __forceinline__ int tiles_of(int len) { return max(1, tile_count(len)); }
 // The tile list is cut by cost: an item (a sequence's row group) costs its tiles and kItemCost
 // more, for its query and its result; those units come before its tiles.
 constexpr int kItemCost = 1;
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     if (threadIdx.x == 0) {
       const int item = blockIdx.x / w.splits, s = blockIdx.x % w.splits;
       const int len = clamp_length(*a.prefix_length, a.prefix_width, a.c, a.status);
-      const int tiles = (len + kTile - 1) / kTile;
+      const int tiles = tile_count(len);
       const int t0 = static_cast<int>(static_cast<int64_t>(tiles) * s / w.splits);
       shared_int[0] = 0;
       shared_int[1] = item;

@@ -61,6 +61,11 @@ __device__ __forceinline__ int quiet_length(int n, int64_t width, int page_shift
   return n < 0 ? 0 : static_cast<int>(n < cap ? n : cap);
 }
 
+// Tiles of that many tokens; lengths go up to 2^31 - 1, so nothing is added to one.
+__host__ __device__ constexpr int tile_count(int len) {
+  return len / kTile + (len % kTile != 0);
+}
+
 // A partial result of `rows` query rows: their maxima (base 2), sums, and outputs before the
 // division, [rows, head_dim].
 __host__ __device__ constexpr int partial_floats(int rows, int head_dim) {

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int len = threadIdx.x == 0 && blockIdx.x == 0
                       ? clamp_length(*a.prefix_length, a.prefix_width, a.c, a.status)
                       : quiet_length(*a.prefix_length, a.prefix_width, a.c.page_shift);
-  const int all = (len + kTile - 1) / kTile;
+  const int all = tile_count(len);
   // at most 2^24 tiles, 64 runs
   const int t0 = static_cast<int>(static_cast<uint32_t>(all * split) / runs);
   const int n = static_cast<int>(static_cast<uint32_t>(all * (split + 1)) / runs) - t0;

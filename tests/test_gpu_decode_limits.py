@@ -33,3 +33,38 @@ def test_layers_are_refused_before_memory_is_taken(fge, t, k):
     with pytest.raises(fge.FgeError, match="fge_moe_layer_decode failed"):
         fge.moe_layer_decode(logits, x, k, 128, *banks)
     assert torch.cuda.max_memory_allocated() - before <= 1 << 17
+
+
+@pytest.mark.parametrize("places", ["own", "prefix", "tcgen05 prefix"])
+@pytest.mark.parametrize("past", [0, 13])
+def test_lengths_up_to_the_last_tokens_below_two_to_the_31(fge, places, past):
+    # a table of as many pages as are admitted, all of them the same one
+    page, d, width = 16, 64, (1 << 27) - 1
+    length = width * page - past
+    g = torch.Generator(device=DEV).manual_seed(5)
+    cache = fge.new_kv_cache(1, page, 1, d, DEV)
+    k, v = (torch.randn((page, 1, d), generator=g, device=DEV).to(torch.bfloat16)
+            for _ in range(2))
+    fge.kv_cache_write(k, v, torch.arange(page, device=DEV), cache)
+    b, heads = (8, 8) if places == "tcgen05 prefix" else (1, 4)
+    q = torch.randn((b, heads, d), generator=g, device=DEV).to(torch.bfloat16)
+    pages = torch.zeros(width, dtype=torch.int32, device=DEV)
+    whole = torch.tensor([length], dtype=torch.int32, device=DEV)
+    lse = torch.empty((b, heads), device=DEV)
+    if places == "own":
+        out = fge.attention_decode(q, cache, pages[None], whole, out_dtype=torch.float32, lse=lse)
+    else:
+        out = fge.attention_decode(q, cache, torch.zeros((b, 1), dtype=torch.int32, device=DEV),
+                                   torch.zeros(b, dtype=torch.int32, device=DEV),
+                                   prefix_pages=pages, prefix_length=whole,
+                                   out_dtype=torch.float32, lse=lse)
+    kd, vd = (a.view(torch.float8_e4m3fn).double()[0, 0] * s.double()[0, 0, :, None]
+              for a, s in ((cache[0], cache[1]), (cache[2], cache[3])))
+    s = q.double() @ kd.T * d ** -0.5
+    want = torch.softmax(s, -1) @ vd
+    # a run of 2^18 tiles adds to its sums 2^18 times, off by 2^-24 at most each, and to its
+    # outputs 2^21 times, off by 2^-23 (sums of matrix instructions are cut off)
+    assert (lse.double() - torch.logsumexp(s, -1) - torch.log(torch.tensor(float(width)))).abs().max() \
+        <= 2.0 ** -6 + 1e-3
+    assert ((out.double() - want).abs() <= (2.0 ** -2 + 2.0 ** -6 + 2.0 ** -11)
+            * (torch.softmax(s, -1) @ vd.abs())).all()
