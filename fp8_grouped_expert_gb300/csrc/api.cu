@@ -807,8 +807,8 @@ static fge_status attention_common(const void* q, int64_t q_stride, int64_t B, i
               FGE_ERR_WORKSPACE_TOO_SMALL);
   NvtxRange range("fge.attention_decode");
   const AttentionArgs a{static_cast<const uint16_t*>(q), q_stride, B, n_heads, c, page_table,
-                        table_width, lengths, shared ? prefix_pages : nullptr, prefix_width,
-                        prefix_length, scale, out_dtype == FGE_DTYPE_F32, out, lse,
+                        table_width, lengths, shared, prefix_pages, prefix_width, prefix_length,
+                        scale, out_dtype == FGE_DTYPE_F32, out, lse,
                         &static_cast<WsHeader*>(ws)->status};
   return from_cuda(
       launch_attention_decode(a, static_cast<uint8_t*>(ws) + kWsHeaderBytes, stream));

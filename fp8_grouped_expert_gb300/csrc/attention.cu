@@ -941,7 +941,7 @@ cudaError_t run_attention(const AttentionArgs& a, void* scratch, cudaStream_t s)
   w.blocks = blocks_of_list();
   const int64_t grid = w.whole ? items : w.blocks;
   cudaError_t e = cudaSuccess;
-  if (a.prefix_pages) {
+  if (a.shared) {
     PrefixPlan p = prefix_plan(a.B, a.n_heads, a.c.n_kv);
     // no more runs than tiles: an empty one still costs the join a look
     const int most = static_cast<int>(
@@ -967,7 +967,7 @@ cudaError_t run_attention(const AttentionArgs& a, void* scratch, cudaStream_t s)
     w.prefix_last = p.last;
     w.prefix_stride = p.stride();
   }
-  const bool dependent = a.prefix_pages != nullptr;
+  const bool dependent = a.shared;
   e = rows == 8 ? launch_attention<D, 8, false>(km, vm, w, grid, dependent, s)
                 : launch_attention<D, 16, false>(km, vm, w, grid, dependent, s);
   if (e != cudaSuccess || (w.whole && !w.prefix_splits)) return e;

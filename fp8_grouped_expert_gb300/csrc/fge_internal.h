@@ -156,7 +156,7 @@ cudaError_t launch_kv_read(const int64_t* slots, int64_t T, const KvCacheArgs& c
                            void* k_out, void* v_out, int32_t* status, cudaStream_t s);
 
 constexpr int64_t kAttentionBatch = 65536, kAttentionRows = 1 << 24;  // B, and below: B n_heads
-// Attention of B single tokens over the cache; prefix_pages null: no shared prefix.
+// Attention of B single tokens over the cache, with `shared` behind a prefix of the whole batch.
 struct AttentionArgs {
   const uint16_t* q;         // [B, n_heads * head_dim], rows q_stride apart
   int64_t q_stride;
@@ -166,7 +166,8 @@ struct AttentionArgs {
   const int32_t* page_table;  // [B, table_width]
   int64_t table_width;
   const int32_t* lengths;     // [B]
-  const int32_t* prefix_pages;
+  bool shared;
+  const int32_t* prefix_pages;  // null if there are none
   int64_t prefix_width;
   const int32_t* prefix_length;
   float scale;

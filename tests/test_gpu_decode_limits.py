@@ -68,3 +68,21 @@ def test_lengths_up_to_the_last_tokens_below_two_to_the_31(fge, places, past):
         <= 2.0 ** -6 + 1e-3
     assert ((out.double() - want).abs() <= (2.0 ** -2 + 2.0 ** -6 + 2.0 ** -11)
             * (torch.softmax(s, -1) @ vd.abs())).all()
+
+
+@pytest.mark.parametrize("b", [2, 40])          # 16-row and tcgen05 form
+@pytest.mark.parametrize("length,code", [(0, 0), (1, 11), (-1, 11), (1 << 30, 11)])
+def test_a_prefix_of_no_pages_is_reported(fge, b, length, code):
+    q, cache, table, lens, _ = _setup(fge, [20, 3] * (b // 2), 16, 4, 128, 64, 2)
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    assert none.data_ptr() == 0
+    ws = fge.new_workspace(fge.workspace_bytes(fge.OP_ATTENTION_DECODE_SHARED, b, 16, 128, 4), DEV)
+    want = fge.attention_decode(q, cache, table, lens)
+    for pages in (none, torch.empty(4, dtype=torch.int32, device=DEV)[:0]):
+        fge.clear_device_status(ws)
+        out = fge.attention_decode(q, cache, table, lens, prefix_pages=pages, workspace=ws,
+                                   prefix_length=torch.tensor([length], dtype=torch.int32,
+                                                              device=DEV))
+        assert fge.read_device_status(ws) == code
+        # an empty prefix adds nothing, though its outputs are joined: one division later
+        assert torch.equal(out, want)
