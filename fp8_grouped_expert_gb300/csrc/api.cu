@@ -738,9 +738,14 @@ static fge_status cache_args(const fge_kv_cache* cache, KvCacheArgs* c) {
   return FGE_OK;
 }
 
-static int32_t* optional_status(void* ws, size_t ws_bytes) {
-  return (ws && ws_bytes >= kWsHeaderBytes && al16(ws)) ? &static_cast<WsHeader*>(ws)->status
-                                                        : nullptr;
+// The status word of a workspace that may be left out.
+static fge_status optional_status(void* ws, size_t ws_bytes, int32_t** status) {
+  *status = nullptr;
+  if (!ws) return FGE_OK;
+  FGE_REQUIRE(al16(ws), FGE_ERR_MISALIGNED);
+  FGE_REQUIRE(ws_bytes >= kWsHeaderBytes, FGE_ERR_WORKSPACE_TOO_SMALL);
+  *status = &static_cast<WsHeader*>(ws)->status;
+  return FGE_OK;
 }
 
 fge_status fge_kv_cache_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -757,9 +762,11 @@ fge_status fge_kv_cache_write(const void* k, int64_t k_stride, const void* v, in
               FGE_ERR_BAD_SHAPE);
   FGE_REQUIRE(al16(k) && al16(v) && (reinterpret_cast<uintptr_t>(slots) & 7u) == 0,
               FGE_ERR_MISALIGNED);
+  int32_t* status;
+  FGE_CHECK(optional_status(ws, ws_bytes, &status));
   return from_cuda(launch_kv_write(static_cast<const uint16_t*>(k), k_stride,
                                    static_cast<const uint16_t*>(v), v_stride, slots, T, c,
-                                   optional_status(ws, ws_bytes), stream));
+                                   status, stream));
 }
 
 fge_status fge_kv_cache_read(const int64_t* slots, int64_t T, const fge_kv_cache* cache,
@@ -774,8 +781,10 @@ fge_status fge_kv_cache_read(const int64_t* slots, int64_t T, const fge_kv_cache
   FGE_REQUIRE(slots && k_out && v_out, FGE_ERR_INVALID_ARG);
   FGE_REQUIRE(al16(k_out) && al16(v_out) && (reinterpret_cast<uintptr_t>(slots) & 7u) == 0,
               FGE_ERR_MISALIGNED);
-  return from_cuda(launch_kv_read(slots, T, c, out_dtype == FGE_DTYPE_F32, k_out, v_out,
-                                  optional_status(ws, ws_bytes), stream));
+  int32_t* status;
+  FGE_CHECK(optional_status(ws, ws_bytes, &status));
+  return from_cuda(launch_kv_read(slots, T, c, out_dtype == FGE_DTYPE_F32, k_out, v_out, status,
+                                  stream));
 }
 
 static fge_status attention_common(const void* q, int64_t q_stride, int64_t B, int n_heads,

@@ -455,7 +455,7 @@ typedef struct {
  * (multiples of 8, at least the row).  slots: [T]; a negative slot is skipped; the others must
  * differ.  Slots past the cache are left out and reported as FGE_ERR_BAD_INDEX, non-finite
  * inputs as FGE_ERR_NONFINITE, in the status word of a workspace of at least 256 bytes
- * (workspace may be NULL: no report).  T may be 0. */
+ * (workspace may be NULL: no report; a smaller or misaligned one is refused).  T may be 0. */
 fge_status fge_kv_cache_write(const void* k_bf16, int64_t k_stride, const void* v_bf16,
                               int64_t v_stride, const int64_t* slots, int64_t T,
                               const fge_kv_cache* cache, void* workspace,

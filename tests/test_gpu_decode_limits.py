@@ -86,3 +86,18 @@ def test_a_prefix_of_no_pages_is_reported(fge, b, length, code):
         assert fge.read_device_status(ws) == code
         # an empty prefix adds nothing, though its outputs are joined: one division later
         assert torch.equal(out, want)
+
+
+def test_a_status_workspace_that_cannot_hold_the_status_is_refused(fge):
+    cache = fge.new_kv_cache(2, 16, 1, 64, DEV)
+    x = torch.ones((2, 64), dtype=torch.bfloat16, device=DEV)
+    slots = torch.arange(2, device=DEV)
+    ws = torch.zeros(512, dtype=torch.uint8, device=DEV)
+    calls = (lambda w: fge.kv_cache_write(x, x, slots, cache, workspace=w),
+             lambda w: fge.kv_cache_read(slots, cache, workspace=w))
+    for call in calls:
+        for w in (None, ws[:256], ws[16:272]):
+            call(w)
+        for w, why in ((ws[:255], "workspace"), (ws[:1], "workspace"), (ws[8:], "align")):
+            with pytest.raises(fge.FgeError, match=why):
+                call(w)
