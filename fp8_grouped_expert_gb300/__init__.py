@@ -809,6 +809,9 @@ class StackedPrefill:
         self.xq = torch.empty((T, H), dtype=torch.uint8, device=dev)
         self.xs = torch.empty((1,), dtype=torch.float32, device=dev)
         self.ws_moe = new_workspace(workspace_bytes(OP_MOE_LAYER, T, H, I, E, k), dev)
+        self.ws_cache = new_workspace(256, dev)
+        for ws in self._workspaces():
+            clear_device_status(ws)
         self.xn = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
         self.q = torch.empty((T, n_heads * 128), dtype=torch.bfloat16, device=dev)
         self.kk = torch.empty((T, kv), dtype=torch.bfloat16, device=dev)
@@ -852,8 +855,16 @@ class StackedPrefill:
             for side in self.side:  # before the next layer rewrites xq, q and kk
                 main.wait_stream(side)
             if caches is not None:
-                kv_cache_write(self.kk, self.v, slots, caches[li])
+                kv_cache_write(self.kk, self.v, slots, caches[li], workspace=self.ws_cache)
         return h
+
+    def _workspaces(self):
+        return [self.ws_lin, self.ws_qt, *self.ws_proj, self.ws_moe, self.ws_cache]
+
+    def status(self):
+        """The first problem that a pass met on the device (0: none), a slot past its cache among
+        them, as a status code; waits for the stream."""
+        return next((s for s in map(read_device_status, self._workspaces()) if s), 0)
 
 
 # ---------------------------------------------------------------------- stacked decode
