@@ -826,7 +826,9 @@ class StackedPrefill:
         selects which layer indices to run (all, in order, by default).  Each residual add
         that a norm follows runs fused with it (fge_residual_rmsnorm, the same bits).  With
         ``caches`` (a KVCache per layer) and ``slots`` (int64 [T]) every layer's keys and
-        values go into its cache, for StackedDecode to go on from."""
+        values go into its cache.  They are this workload's own: its attention is a stand-in and
+        its activation scales are per tensor, so from the second layer on they are not those that
+        StackedDecode computes for the same tokens (which takes a prompt in steps)."""
         order = list(range(len(self.layers)) if layers is None else layers)
         if not order:
             return h
@@ -877,7 +879,8 @@ class StackedDecode:
 
     layers: as StackedPrefill takes them.  ``caches`` holds a KVCache per layer; one page
     table and one list of slots serve all of them.  Activations are scaled by row, so that a
-    sequence's codes do not depend on the others of its batch.  A step launches on the
+    sequence's codes do not depend on the others of its batch; the weights of q, k and v, projected
+    at once, share one scale, where StackedPrefill has three.  A step launches on the
     current stream, allocates nothing and reads nothing back: it can be captured in a graph
     and replayed while the lengths, slots and page table change in place."""
 
@@ -922,7 +925,9 @@ class StackedDecode:
         """h: float32 [B, H], updated in place and returned; slots int64 [B]: where the new
         tokens go (negative: nowhere); page_table int32 [B, width] and lengths int32 [B]: each
         sequence's own tokens, the new one included; prefix_pages, prefix_length: as
-        attention_decode."""
+        attention_decode.  Rows may also be tokens of one sequence, as of a prompt: all of a
+        step's keys and values are written before any is read, and each row's length ends with
+        its own token."""
         b = h.shape[0]
         if not 1 <= b <= self.max_batch:
             raise FgeError("a step takes 1 to %d sequences" % self.max_batch)
