@@ -61,9 +61,9 @@ __device__ __forceinline__ int quiet_length(int n, int64_t width, int page_shift
   return n < 0 ? 0 : static_cast<int>(n < cap ? n : cap);
 }
 
-// Tiles of that many tokens; lengths go up to 2^31 - 1, so nothing is added to one.
+// Tiles of that many tokens; unsigned, as lengths go up to 2^31 - 1.
 __host__ __device__ constexpr int tile_count(int len) {
-  return len / kTile + (len % kTile != 0);
+  return static_cast<int>((static_cast<uint32_t>(len) + kTile - 1) / kTile);
 }
 
 // A partial result of `rows` query rows: their maxima (base 2), sums, and outputs before the
