@@ -16,6 +16,8 @@
 // 2^(x - M) vs begins at 1 at most; l sums 2^(x - M).  The next tiles keep M and only bound what
 // they got, by their sum and the largest value scale; a tile that may pass 2^15 is done over with
 // a new M.  Tokens of value zero count in l alone: a zero row's scale would set M for the others.
+// vs is in units of the power of two of the run's first tile's largest, so that l keeps its range
+// whatever the size of the values; one below 2^-90 of that is lost.
 //   Bound by the exchange between tensor core and softmax: a token tile takes a block 3 us, of
 // which the 32 MMAs are 1.1 (64 cycles each).  Measured for a batch of 96 (384 rows a head, 4
 // heads) behind 16384 tokens, own tokens and join included: one softmax warpgroup a row tile and
@@ -154,6 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* s_int = reinterpret_cast<int*>(sm + L::kBars + kBarCount * 8);
   volatile int* s_abort = s_int;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_int + 1);
+  float* s_unit = reinterpret_cast<float*>(s_int + 2);  // of the value scales
+  float* s_most = reinterpret_cast<float*>(s_int + 4);  // largest scale of each value warp
   const AttentionArgs& a = w.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](int i) { return bars + 8 * i; };
@@ -318,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     load(t0);
+    float down = 1.0f;  // 1 / *s_unit
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
       if (i > 1) wait(kValueEmpty + st, (i >> 1) - 1);
@@ -334,9 +339,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = __reduce_or_sync(0xffffffffu, m << (lane / kWords * 8));
         if (lane / kPer == u) some = m >> (lane % kPer) & 1u;
       }
-      const float weight = some ? vs : 0.0f;
+      float weight = some ? vs : 0.0f;
+      if (i == 0) {
+        float most = fabsf(weight);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+        if (lane == 0) s_most[warp - kValueWarp] = most;
+        asm volatile("bar.sync 3, %0;" ::"n"(kConvert) : "memory");
+        most = fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3]));
+        // biased exponents, both factors normal
+        const uint32_t e = min(253u, __float_as_uint(most) >> 23);
+        if (e) down = __uint_as_float((254u - e) << 23);
+        if (tid == 0) *s_unit = e ? __uint_as_float(e << 23) : 1.0f;
+      }
+      weight *= down;
       float* sc = reinterpret_cast<float*>(sm + L::kScale + st * L::kScaleBytes);
-      // a very small scale must not let the sum of 2^(x - M) overflow
+      // a scale far below the others must not let the sum of 2^(x - M) overflow
       sc[kTile + token] = here ? fmaxf(log2f(fabsf(weight)), -90.0f) : -INFINITY;
       sc[2 * kTile + token] = weight;
       float most = fabsf(weight);
@@ -613,6 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         part[kRows + row] = l + tops[row];
       }
       float* o = part + 2 * kRows + row * D + half * (D / 2);
+      const float unit = *s_unit;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         uint32_t r[32];
@@ -621,10 +640,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live)
 #pragma unroll
           for (int j = 0; j < 32; j += 8)  // whole sectors
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
                              o + 32 * c + j),
-                         "r"(r[j]), "r"(r[j + 1]), "r"(r[j + 2]), "r"(r[j + 3]), "r"(r[j + 4]),
-                         "r"(r[j + 5]), "r"(r[j + 6]), "r"(r[j + 7])
+                         "f"(__uint_as_float(r[j]) * unit), "f"(__uint_as_float(r[j + 1]) * unit),
+                         "f"(__uint_as_float(r[j + 2]) * unit),
+                         "f"(__uint_as_float(r[j + 3]) * unit),
+                         "f"(__uint_as_float(r[j + 4]) * unit),
+                         "f"(__uint_as_float(r[j + 5]) * unit),
+                         "f"(__uint_as_float(r[j + 6]) * unit),
+                         "f"(__uint_as_float(r[j + 7]) * unit)
                          : "memory");
       }
     }

@@ -129,3 +129,17 @@ def test_tiny_queries_and_large_keys(fge, prefix, b, d, power):
     # the row's factor may be subnormal: 2^-129 keeps 20 bits
     _check(fge, s, prefix, scale=0.25 * 2.0 ** (-118 - power),
            unit=tight.TCGEN05 if b * 4 >= 64 else tight.OWN, score_error=2.0 ** -19)
+
+
+@pytest.mark.parametrize("prefix,b", [(None, 3), (3000, 3), (3000, 40)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power", [-112, -95, -60, 60, 110])
+def test_values_of_any_size(fge, prefix, b, d, power):
+    # scales from 2^-122 to 2^110, rows of value zero (scale 1) among them
+    s = _setup(fge, [(97 * i) % 300 for i in range(b)], 16, 4, d, 64, 31, prefix, spoil=False)
+    cache = s[1]
+    some = (cache[2] & 0x7F).amax(-1) != 0
+    cache[3][some] *= 2.0 ** power
+    # the own part's weights are brought up by 2^126 at most: from 2^-118 to 2^8 instead of 2^14
+    own = tight.OWN if power > -100 else 2.0 ** -33
+    _check(fge, s, prefix, unit=tight.TCGEN05 if b * 4 >= 64 else own)
