@@ -565,7 +565,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t sum2 = 0;
 #pragma unroll
         for (int c = 0; c < kHalfTile / 16; ++c) {
-          const uint32_t mask = (c < 2 ? here.x : here.y) >> (c & 1) * 16;
           uint32_t r[16];
           tmem_ld_32x32b_x16(scores + 16 * c, r);
           wait_ld16(r);
@@ -580,6 +579,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               e.x = exp2_approx(e.x);
               e.y = exp2_approx(e.y);
               if (!full) {
+                // read again: in registers all the time, it made the loop spill 13 of them
+                const uint32_t mask = reinterpret_cast<const volatile uint32_t*>(
+                                          scales + 3 * kTile)[2 * half + (c >> 1)] >>
+                                      (c & 1) * 16;
                 if (!(mask >> (j + 2 * h) & 1u)) e.x = 0.0f;
                 if (!(mask >> (j + 2 * h + 1) & 1u)) e.y = 0.0f;
               }

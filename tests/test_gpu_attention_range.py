@@ -143,3 +143,27 @@ def test_values_of_any_size(fge, prefix, b, d, power):
     # the own part's weights are brought up by 2^126 at most: from 2^-118 to 2^8 instead of 2^14
     own = tight.OWN if power > -100 else 2.0 ** -33
     _check(fge, s, prefix, unit=tight.TCGEN05 if b * 4 >= 64 else own)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_tcgen05_prefix_within_the_tight_bounds(fge, d):
+    s = _setup(fge, [(11 * i) % 90 for i in range(40)], 16, 4, d, 64, 29, 5000, spoil=False)
+    _check(fge, s, 5000, unit=tight.TCGEN05)
+
+
+def test_tcgen05_prefix_gives_the_same_bits_every_time(fge):
+    # full-size runs of the kernel whose values come from TMEM: 384 rows a head, three row-tile
+    # pairs, and an odd last one
+    for b in (96, 72):
+        q, cache, table, lens, pp = _setup(fge, [(31 * i) % 200 for i in range(b)], 16, 4, 128, 64,
+                                           b, 9000, spoil=False)
+        pl = torch.tensor([9000], device=DEV, dtype=torch.int32)
+        lse = torch.empty((b, 16), device=DEV)
+
+        def call():
+            return fge.attention_decode(q, cache, table, lens, prefix_pages=pp, prefix_length=pl,
+                                        out_dtype=torch.float32, lse=lse)
+
+        want, first = call(), lse.clone()
+        for _ in range(50):
+            assert torch.equal(call(), want) and torch.equal(lse, first)
