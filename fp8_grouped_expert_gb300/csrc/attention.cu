@@ -10,8 +10,8 @@
 // output, joined at the end.
 //   Scores.  mma m16n8k16 on the keys widened to fp16 (exact; an e4m3 MMA of this size takes its
 // operands apart into fp16 as well, both of them and every time).  The query is an fp16 value
-// too: a power of two brings the row's largest to [128, 256), and the 8 significant bits of a
-// bf16 value fit down to 2^-31 of that.
+// too: a power of two brings the row's largest to [128, 256); the 8 significant bits of a bf16
+// value fit down to 2^-24 of that, and smaller values are off by 2^-32 of it at most.
 //   Output.  mma m16n8k16 on the values widened to fp16 (exact); p * vs is rounded to fp16
 // (2^-11) after a power of two that keeps the largest that the row has had from this warp, as
 // weighted against the present maximum, in [2^14, 2^15): what is lost lies below 2^-39 of it,
@@ -20,10 +20,10 @@
 // that ragged batches and one long sequence fill the GPU alike; a sequence that a cut divides
 // leaves partial results (maximum, sum, output) that a second kernel joins in order.
 //   Bound by how fast the tiles come: 64 sequences of up to 16383 tokens (16 heads on 4, 318 MB)
-// take 67 us, 54 of them in this kernel (5.9 TB/s: two blocks an SM with three tiles of 34 KB each
-// in flight; scores and outputs keep its issue slots 37% and the MMA unit 25% busy); one of 131071
+// take 67 us, 54 of them in this kernel (5.8 TB/s: two blocks an SM with three tiles of 34 KB each
+// in flight; scores and outputs keep its issue slots 41% and the MMA unit 25% busy); one of 131071
 // tokens (138 MB) 35 us, 26 of them here, 4 of those before the first tile.  Short sequences are
-// bound by the chain length, page number, tile, result: 300 tokens 6 us.
+// bound by the chain length, page number, tile, result: 300 tokens 6.2 us.
 #include "attention.cuh"
 
 namespace fge {

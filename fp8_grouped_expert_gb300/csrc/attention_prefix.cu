@@ -23,7 +23,7 @@
 // heads) behind 16384 tokens, own tokens and join included: one softmax warpgroup a row tile and
 // two looks at the scores 66 us; two warpgroups and one look, whole rows of the query loaded by
 // neighbouring lanes (a row a lane, 16 bytes a time, read the query's sectors several times)
-// 60 us; now 53 us, of which this kernel is about 30.
+// 60 us; now 54 us, of which this kernel is about 30.
 #include "attention.cuh"
 
 namespace fge {
